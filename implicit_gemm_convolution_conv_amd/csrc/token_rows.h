@@ -257,7 +257,7 @@ __device__ __attribute__((always_inline)) inline unsigned row_max(unsigned v, un
 // 8-bit codes of a row. The row maximum a = max |v| is taken over bit patterns
 // (non-negative floats order like them, and a NaN comes out on top), floored at
 // 2^-100 so that neither quotient overflows; scale = a / top, code =
-// round-to-nearest-even(v * (top / a)), top = 127 (int8) or 448 (E4M3FN). A row
+// round-to-nearest-even(fp32(v * (top / a))), top = 127 (int8) or 448 (E4M3FN). A row
 // with an infinity or a NaN gets the scale NaN and zero codes: all of it
 // dequantises to NaN.
 template <Elem OUT>
@@ -272,13 +272,16 @@ struct RowCodes {
         scale = finite ? __fdiv_rn(a, top) : __uint_as_float(0x7fc00000u);
         inv = finite ? __fdiv_rn(top, a) : 0.0f;
     }
-    // Codes of 8 elements. int8: adding 1.5 * 2^23 rounds v * inv (|v * inv| <=
-    // 127 * (1 + 2^-23)) to an integer in the low mantissa bits, whose low byte
-    // is the code in two's complement; the fma rounds once. fp8: the hardware
-    // conversion; 448 * (1 + 2^-23) still rounds to 448. A zero `inv` (a row
-    // that is not finite) gives zero codes without looking at v.
+    // Codes of 8 elements, of the product v * inv rounded to fp32. int8: adding
+    // 1.5 * 2^23 rounds the product (at most 127 * (1 + 2^-23)) to an integer in
+    // the low mantissa bits, whose low byte is the code in two's complement. One
+    // fma would decide ties by the error of inv: v = a / 2, on the tie 63.5, is
+    // common in bf16 rows. fp8: the hardware conversion; 448 * (1 + 2^-23) still
+    // rounds to 448. A zero `inv` (a row that is not finite) gives zero codes
+    // without looking at v.
     __device__ __attribute__((always_inline)) u32x2 codes(const float (&v)[8]) const
     {
+#pragma clang fp contract(off)
         u32x2 c = {0, 0};
         if (inv == 0.0f)
             return c;
@@ -288,7 +291,7 @@ struct RowCodes {
                 unsigned b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    b[e] = __float_as_uint(fmaf(v[4 * i + e], inv, 12582912.0f));
+                    b[e] = __float_as_uint(v[4 * i + e] * inv + 12582912.0f);
                 const unsigned lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
                 const unsigned hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
                 c[i] = lo | hi;

@@ -357,7 +357,7 @@ IGC_API int conv_debug_force_tap_raster(int mode);
  *
  * 8-bit rows. Codes are int8 or fp8 E4M3FN with one fp32 scale for each row:
  * value = code * scale. With a = the row's largest magnitude, floored at 2^-100,
- *   scale = fp32(a / top), code = nearest(v * fp32(top / a)), ties to even,
+ *   scale = fp32(a / top), code = nearest(fp32(v * fp32(top / a))), ties to even,
  * top = 127 (int8; -128 is not used) or 448 (fp8). A row that holds an infinity
  * or a NaN gets the scale NaN and zero codes, so that all of it reads as NaN.
  * Rows of codes are padded with zeros to linear_packed_cols(cols) elements, their
