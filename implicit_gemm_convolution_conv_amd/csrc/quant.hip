@@ -27,16 +27,46 @@ __device__ __attribute__((always_inline)) inline float exp_f32(float x)
     return fmaf(b * e, 0x1.62e43p-1f, b);
 }
 
-// g / (1 + exp(-g)). The exponent is kept within [-90, 80]: beyond 80 the
-// quotient is under 1e-33 * g, below -90 the sum is 1, and no infinity enters
-// the remainder term above. The reciprocal's quotient is corrected once by its
-// remainder: each of these roundings moves a code now and then.
+// g / (1 + exp(-g)) for g >= kGateTail. The exponent is kept above -90, where the
+// sum is 1, and no infinity enters the remainder term above. The reciprocal's
+// quotient is corrected once by its remainder: each of these roundings moves a code
+// now and then.
+constexpr float kGateTail = -80.0f;
+
 __device__ __attribute__((always_inline)) inline float silu(float g)
 {
-    const float d = 1.0f + exp_f32(__builtin_amdgcn_fmed3f(-g, -90.0f, 80.0f));
+    const float d = 1.0f + exp_f32(fmaxf(-g, -90.0f));
     const float r = __builtin_amdgcn_rcpf(d);
     const float q = g * r;
     return fmaf(fmaf(-d, q, g), r, q);
+}
+
+// silu(g) * u for g below kGateTail, where 1 + exp(-g) is exp(-g) in fp32: g exp(g)
+// u as (g e)(e u), e = exp(g / 2). The reciprocal above would leave fp32's range
+// from -88 on; e does so below -174, where the result is under 2^-100 whatever u
+// is. Gates down to the type's lowest value give zero.
+__device__ __attribute__((always_inline)) inline float gated_tail(float g, float u)
+{
+    const float e = exp_f32(fmaxf(0.5f * g, -100.0f));
+    return (g * e) * (e * u);
+}
+
+// v = silu(v) * u for a run. Few rows hold gates below kGateTail: a wave without
+// them skips that part.
+__device__ __attribute__((always_inline)) inline void gate(float (&v)[8], const float (&u)[8])
+{
+    float low = v[0], g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        low = fminf(low, v[i]);
+        g[i] = v[i];
+        v[i] = silu(g[i]) * u[i];
+    }
+    if (__any(low < kGateTail)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = g[i] < kGateTail ? gated_tail(g[i], u[i]) : v[i];
+    }
 }
 
 // The row's values stay in registers between its maximum and its codes (gate and up
@@ -62,9 +92,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void linear_quant_kernel(Qua
         if constexpr (GLU) {
             float u[8];
             Run<T>::load(x + p.cols + k, p.cols - k, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = silu(v[i]) * u[i];
+            gate(v, u);
         }
     };
     unsigned m = 0;
@@ -86,9 +114,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void linear_quant_kernel(Qua
             if constexpr (GLU) {
                 float u[8];
                 ru.unpack(c, p.cols, t, u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[c][i] = silu(v[c][i]) * u[i];
+                gate(v[c], u);
             }
             top(v[c]);
         }
