@@ -243,7 +243,9 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void norm_bwd_kernel(NormBwdParam
             for (int i = 0; i < 8; ++i)
                 ss = fmaf(h[c][i], h[c][i], ss);
         ss = row_sum<TPR>(ss, red[flip][0]);
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.cols) + p.eps));
+        // a row past the last adds nothing to dw: its rstd would be infinite with eps = 0, and 0 * inf is NaN
+        const float rstd = RPB > 1 && row >= p.rows ? 0.0f
+                                                    : __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.cols) + p.eps));
         float gn = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
