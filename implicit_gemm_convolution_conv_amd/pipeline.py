@@ -3,9 +3,17 @@
 This module only orders calls into the library (amax -> scales -> pack ->
 conv; norm -> codes -> linear) and allocates their outputs; it performs no
 arithmetic of its own.
+
+stream: a torch stream or a raw handle (default: torch's current stream). Work
+on it is as under ``torch.cuda.stream(stream)``: outputs and scratch come from
+the allocator's pool of that stream, so that no block is handed out again while
+the stream still works on it. What the inputs wait for, and who else uses the
+outputs, is the caller's to order, as with torch's own operations.
 """
 
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -19,12 +27,22 @@ def _code(dtype):
     return DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
 
 
+def _allocating(stream, device):
+    """The context in which buffers for work on `stream` are allocated."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def packed_weight(w_kctrs: torch.Tensor, dtype="bf16", x_layout="NDHWC", scale_pair=None, stream=None):
     """Pack a bf16 KCTRS filter (fp8: scale_pair must hold its {s, inv})."""
     dt = _code(dtype)
     cols = B.conv_packed_w_cols(w_kctrs.shape, dt)
-    out = torch.empty((w_kctrs.shape[0], cols), dtype=torch.uint8 if dt == B.IGC_FP8_E4M3FN else torch.bfloat16,
-                      device=w_kctrs.device)
+    with _allocating(stream, w_kctrs.device):
+        out = torch.empty((w_kctrs.shape[0], cols), dtype=torch.uint8 if dt == B.IGC_FP8_E4M3FN else torch.bfloat16,
+                          device=w_kctrs.device)
     B.conv_pack_w(w_kctrs, out, w_kctrs.shape, dt, LAYOUTS[x_layout], scale_pair, stream)
     return out
 
@@ -33,16 +51,18 @@ def packed_input(x_ncdhw: torch.Tensor, dtype="bf16", scale_pair=None, stream=No
     """NCDHW bf16 -> NDHWC (bf16 or fp8 codes), returned as a (N, D, H, W, C) tensor."""
     dt = _code(dtype)
     n, c, d, h, w = x_ncdhw.shape
-    out = torch.empty((n, d, h, w, c), dtype=torch.uint8 if dt == B.IGC_FP8_E4M3FN else torch.bfloat16,
-                      device=x_ncdhw.device)
+    with _allocating(stream, x_ncdhw.device):
+        out = torch.empty((n, d, h, w, c), dtype=torch.uint8 if dt == B.IGC_FP8_E4M3FN else torch.bfloat16,
+                          device=x_ncdhw.device)
     B.conv_pack_x(x_ncdhw, out, x_ncdhw.shape, dt, scale_pair, stream)
     return out
 
 
 def fp8_scales(x_bf16: torch.Tensor, w_bf16: torch.Tensor, stream=None):
     """Device float[4] = {s_x, inv_x, s_w, inv_w} from the two tensors' amax."""
-    amax = torch.empty(2, dtype=torch.float32, device=x_bf16.device)
-    scales = torch.empty(4, dtype=torch.float32, device=x_bf16.device)
+    with _allocating(stream, x_bf16.device):
+        amax = torch.empty(2, dtype=torch.float32, device=x_bf16.device)
+        scales = torch.empty(4, dtype=torch.float32, device=x_bf16.device)
     B.conv_amax(x_bf16, x_bf16.numel(), amax[0:1], stream)
     B.conv_fp8_scales(amax[0:1], scales[0:2], stream)
     B.conv_amax(w_bf16, w_bf16.numel(), amax[1:2], stream)
@@ -68,7 +88,8 @@ def conv3d(x_ncdhw: torch.Tensor, w_kctrs: torch.Tensor, stride=(1, 1, 1), pad=(
     scales = fp8_scales(x_ncdhw, w_kctrs, stream) if dt == B.IGC_FP8_E4M3FN else None
     sx = scales[0:2] if scales is not None else None
     sw = scales[2:4] if scales is not None else None
-    y = output(xshape, wshape, stride, pad, dil, x_ncdhw.device)
+    with _allocating(stream, x_ncdhw.device):
+        y = output(xshape, wshape, stride, pad, dil, x_ncdhw.device)
     if direct:
         wp = packed_weight(w_kctrs, dt, "NCDHW", sw, stream)
         B.conv_fwd(x_ncdhw, wp, y, xshape, wshape, stride, pad, dil, dt, B.IGC_NCDHW, scales, stream)
@@ -141,7 +162,8 @@ def quantised(x: torch.Tensor, kind="int8", glu=False, stream=None) -> Codes:
     if glu and wide % 2:
         raise ValueError(f"a gated row holds two halves, got {wide} elements")
     cols = wide // 2 if glu else wide
-    q = Codes(rows, cols, kind, x.device)
+    with _allocating(stream, x.device):
+        q = Codes(rows, cols, kind, x.device)
     B.linear_quant(x, _row_stride(x, rows, wide, "x"), q.codes, q.ld, q.scales, rows, cols, _value_type(x), q.kind,
                    B.IGC_ACT_SILU_GLU if glu else B.IGC_ACT_NONE, stream)
     return q
@@ -154,13 +176,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps=1e-6, kin
     for t, name in ((residual, "residual"), (weight, "weight")):
         if t is not None and t.dtype != x.dtype:
             raise TypeError(f"{name} must be {x.dtype} like x, got {t.dtype}")
-    h = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if residual is not None else None
-    if kind is None:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        out, ld, scales, y_type = y, cols, None, dt
-    else:
-        y = Codes(rows, cols, kind, x.device)
-        out, ld, scales, y_type = y.codes, y.ld, y.scales, y.kind
+    with _allocating(stream, x.device):
+        h = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if residual is not None else None
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if kind is None else Codes(rows, cols, kind, x.device)
+    out, ld, scales, y_type = (y, cols, None, dt) if kind is None else (y.codes, y.ld, y.scales, y.kind)
     B.norm_fwd(x, _row_stride(x, rows, cols, "x"), residual, _row_stride(residual, rows, cols, "residual"),
                _vector(weight, cols, x.dtype, "weight"), h, cols, out, ld, scales, rows, cols, eps, dt, y_type, stream)
     return y, (x if h is None else h)
@@ -174,9 +193,10 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dres=
     for t, name in ((dy, "dy"), (dres, "dres"), (weight, "weight")):
         if t is not None and t.dtype != h.dtype:
             raise TypeError(f"{name} must be {h.dtype} like h, got {t.dtype}")
-    dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
-    dw = torch.empty((cols,), dtype=torch.float32, device=h.device)
-    ws = torch.empty((B.norm_bwd_workspace_bytes(rows, cols),), dtype=torch.uint8, device=h.device)
+    with _allocating(stream, h.device):
+        dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
+        dw = torch.empty((cols,), dtype=torch.float32, device=h.device)
+        ws = torch.empty((B.norm_bwd_workspace_bytes(rows, cols),), dtype=torch.uint8, device=h.device)
     B.norm_bwd(dy, _row_stride(dy, rows, cols, "dy"), h, _row_stride(h, rows, cols, "h"),
                _vector(weight, cols, h.dtype, "weight"), dres, _row_stride(dres, rows, cols, "dres"), dx, cols, dw, rows,
                cols, eps, dt, ws, None, stream)
@@ -190,9 +210,10 @@ def linear(a: Codes, w: Codes, bias=None, out_dtype=torch.bfloat16, out=None, st
     if a.cols != w.cols:
         raise ValueError(f"reduction lengths differ: {a.cols} and {w.cols}")
     m, n, k = a.rows, w.rows, a.cols
-    y = torch.empty((m, n), dtype=out_dtype, device=a.codes.device) if out is None else out
-    nws = B.linear_fwd_workspace_bytes(m, n, k, a.kind, _value_type(y))
-    ws = torch.empty((nws,), dtype=torch.uint8, device=a.codes.device) if nws else None
+    with _allocating(stream, a.codes.device):
+        y = torch.empty((m, n), dtype=out_dtype, device=a.codes.device) if out is None else out
+        nws = B.linear_fwd_workspace_bytes(m, n, k, a.kind, _value_type(y))
+        ws = torch.empty((nws,), dtype=torch.uint8, device=a.codes.device) if nws else None
     B.linear_fwd(a.codes, a.ld, a.scales, w.codes, w.ld, w.scales, _vector(bias, n, torch.float32, "bias"), y,
                  _row_stride(y, m, n, "out"), m, n, k, a.kind, _value_type(y), ws, None, stream)
     return y
