@@ -24,10 +24,12 @@ typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 // PRECISE matters for fp8: within one fp8 instruction (any width) products are
 // aligned to the largest of them and lose what falls about 13 bits below it
 // (measured: up to 2^-11.4 of the largest product, 4e-5 of the result's 2-norm on
-// codes of mixed exponents); the running sum itself is fp32. That is far below a
-// bf16 output's rounding of 2^-8 and the codes' own 2^-4, so bf16 outputs take it;
-// an fp32 output gets the exact codes widened to bf16 and the bf16 instruction, at
-// half the rate.
+// codes of mixed exponents); the running sum itself is fp32. Where large products
+// do not cancel, that is far below a bf16 output's rounding of 2^-8 and the codes'
+// own 2^-4, so bf16 outputs take it; where they do, as with outlier channels of
+// opposite signs, it may be more than the small result itself. An fp32 output gets
+// the exact codes widened to bf16 and the bf16 instruction, at half the rate: that
+// is the way to fp32 sums, and the header says so.
 template <Elem T, bool PRECISE>
 struct Mma;
 

@@ -419,8 +419,15 @@ IGC_API int linear_quant(const void *x, int64_t ldx, void *q, int64_t ldq, float
  * Linear layer on 8-bit operands:
  *   y[i][j] = acc * a_scales[i] * w_scales[j] + bias[j], acc = sum_k a[i][k] * w[j][k]
  * for m tokens a and n output channels w, rounded once to y_dtype (IGC_BF16 or
- * IGC_F32). acc is exact for int8 (int32; k <= 131071) and fp32 for fp8; the
- * scales and the bias are applied in fp32.
+ * IGC_F32). The scales and the bias are applied in fp32. acc is exact for int8
+ * (int32; k <= 131071). For fp8, y_dtype chooses its precision as well:
+ *   IGC_F32   exact products, summed in fp32, at half the matrix rate;
+ *   IGC_BF16  the fp8 matrix instruction, which aligns 128 products to the largest
+ *             of them and loses what falls about 13 bits below: acc, a running
+ *             fp32 sum of these, is off by up to 2^-11 of the largest product for
+ *             every 128 codes. Without cancellation that is far below bf16's own
+ *             rounding; where large products cancel (two outlier channels of
+ *             opposite sign) it may exceed what is left, and IGC_F32 avoids it.
  *  dtype    IGC_INT8 or IGC_FP8_E4M3FN, of a and w alike; rows as linear_quant
  *           leaves them, row strides up to 2^22 codes.
  *  bias_dev NULL or fp32[n].
