@@ -40,10 +40,7 @@ __device__ __attribute__((always_inline)) inline void store_piece(const LinearPa
     constexpr int PER = 16 / sizeof(U);
     U *dst = static_cast<U *>(p.y) + (int64_t)m * p.ldy + n;
     if (n + PER <= p.n) {
-        if (p.stream_out)
-            __builtin_nontemporal_store(v, reinterpret_cast<V *>(dst));
-        else
-            *reinterpret_cast<V *>(dst) = v;
+        *reinterpret_cast<V *>(dst) = v;
     } else {
 #pragma unroll
         for (int e = 0; e < PER; ++e)

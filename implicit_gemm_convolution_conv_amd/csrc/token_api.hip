@@ -436,10 +436,6 @@ int linear_fwd(const void *a, int64_t lda, const float *a_scales_dev, const void
     p.splits = pl.splits;
     p.ksplit = pl.ksplit;
     p.group = pl.group;
-    // Outputs leave past the L2 cache, which then keeps more of both operands (8192^3 fp8 403 us, 419 us through
-    // it), except large ones of short reductions, whose time is the writing: the cache evens that out
-    // (9500 x 10240 x 1280 fp8 130.2 us, 133.8 us past it).
-    p.stream_out = pl.nk > 16 || m * n <= int64_t(32) << 20;
     p.part = workspace_dev;
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = pl.tile == LT_SKINNY

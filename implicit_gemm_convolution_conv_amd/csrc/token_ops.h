@@ -70,7 +70,6 @@ struct LinearParams {
     int nk;                  // reduction steps of 128 codes
     int tiles_m, tiles_n;
     int group;               // token tiles a raster group walks together
-    int stream_out;          // outputs past the caches
     int splits, ksplit;      // split j runs steps [j * ksplit, min(nk, (j + 1) * ksplit))
     void *part;              // splits > 1: sums [split][m][n], int32 (int8 codes) or fp32 (fp8)
 };
