@@ -61,10 +61,13 @@ __device__ __attribute__((always_inline)) inline void store_piece(const LinearPa
 // 2730 TFLOP/s, int8 419 us, 2620 TOP/s, the units 67 % busy at 2.0 and 1.8 GHz; on
 // codes that are all zero 355 and 342 us; fp8 widened for fp32 outputs 750 us, 1470
 // TFLOP/s); short reductions their outputs as well
-// (9500 x 10240 x 1280 int8 to bf16 135 us, of which writing 195 MB takes 44); few
-// tokens the weight's way from HBM (48 x 8192 x 8192 fp8 13.0 us, 5.2 TB/s); small
-// ones a launch and the latency of each step (777 x 1283 x 1291 int8 to fp32, 64 x 128
-// tiles, 7.1 us, 11 steps of 0.3 us after 1.7).
+// (9500 x 10240 x 1280 int8 to bf16 135 us, of which writing 195 MB takes 44; the
+// fewer the steps, the more: 8000 x 8000 x 512 int8 to fp32 84 us, 264 MB, one
+// workgroup a CU whose outputs go with no loads beside them); few tokens the weight's
+// way into the CUs (48 x 8192 x 8192 fp8 19 us from HBM, 3.5 TB/s; 13 to 14 us where
+// the 256 MB cache holds the weight); small ones a launch and the latency of each step
+// (777 x 1283 x 1291 int8 to fp32, 64 x 128 tiles, 7.1 us, 11 steps of 0.3 us after
+// 1.7).
 template <Elem T, Elem OUT, int BN, int BM, int WN, int WM, int SW, int SA, int SPREAD>
 __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinearParams p)
 {

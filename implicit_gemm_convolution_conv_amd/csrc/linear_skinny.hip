@@ -6,11 +6,11 @@
 // w + 8, ... Every byte of its operands is used by one wave only, so it goes
 // straight from memory (or the caches) into the registers of the matrix
 // instruction, without LDS. The waves' sums meet in LDS at the end and are added in
-// wave order. No workspace and no second launch. 1 x 1280 x 5120 int8: 5.3 us
-// against 7.0 us on 32 x 32 tiles (40 of them); 16 x 2048 x 8192 fp8: 9.4 against
-// 11.0 us (64 of them); with 256 of them (1 x 8192 x 8192) those are ahead, 11.9
-// against 12.8 us, until the weight is too large to stay in the caches: 1 x 32768 x
-// 8192 fp8 46.6 us, 5.8 TB/s, against 52.7 us. Loading a second register set ahead
+// wave order. No workspace and no second launch. Against the best other tile, weights
+// from HBM (enough of them in turn that no cache holds one): 1 x 1280 x 5120 int8 6.6
+// us, 8.4 on 32 x 32 tiles; 1 x 8192 x 8192 fp8 14.9 and 16.1 us; 1 x 32768 x 8192
+// 47.4, 5.7 TB/s, and 55.4. Weights that the 256 MB cache holds: 5.1 and 6.4, 12.8
+// and 12.3 us; the last is too large for that. Loading a second register set ahead
 // lost 1 us.
 #include "linear.h"
 

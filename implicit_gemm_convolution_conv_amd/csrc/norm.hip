@@ -14,8 +14,9 @@
 // along the residual stream. All sums are fp32.
 //
 // Every operand is read once and every result written once, a few operations a
-// byte: HBM bandwidth bounds both directions (a copy reaches 4.8 TB/s on the same
-// card), and one row on its own is a launch and its dependent trips to memory.
+// byte: HBM bandwidth bounds both directions, and one row on its own is a launch and
+// its dependent trips to memory. A copy of 4 GiB reaches 4.8 TB/s on the same card;
+// that is no upper bound: these kernels read more than they write, and go to 5.8.
 #include <algorithm>
 #include <type_traits>
 

@@ -92,6 +92,11 @@ int done(const char *fn, hipError_t e)
 // to sum, both types) on every tile: choosing by it is 1.6 % slower than the best
 // tile of each shape on average. fp8 codes widened to bf16 (fp32 outputs) cost
 // `widened` times as much a step, fitted to 220 more (0.7 % slower than their best).
+// Two sets of operands in turn were timed: weights of those shapes, 84 MB at most, come
+// from the 256 MB cache. From HBM a few tokens take longer on every tile (1 x 8192 x
+// 8192 fp8 14.9 us, 12.8 from the cache; 48 x 8192 x 8192 19.0 and 13.8) and the choice
+// is within 3 % of the best tile on those tried but 4 x 8192 x 8192 (16.2 us, 15.4 on
+// 16 x 16).
 struct TileCost {
     int bn, bm;  // features x tokens
     double step, round, shared, widened;
@@ -156,13 +161,14 @@ double linear_cost(int t, int64_t m, int64_t tiles, int64_t steps, bool widened,
     return kLaunch + (rounds > 1.0 ? rounds * c.shared : 1.0) * ((double)steps * c.step * (widened ? c.widened : 1.0) + c.round);
 }
 
-// A few tokens over a weight that comes from HBM, too large for the 256 MB cache to
-// keep: the time is the weight's way into the CUs, and the 16 x 16 workgroups, whose
-// waves wait for no barrier, take it fastest (1 x 16384 x 8192 fp8 23.9 us, 33.6 us on
-// the best of the other tiles; 1 x 60000 x 4096 43.8 and 48.5; 4 x 32768 x 8192 48.7 and
-// 54.7), where their waves' rounds of loads are nearly full (1 x 30000 x 5120, 40 steps
-// in rounds of 32: over 34 us, 30.6 us by cost) and the tokens' rows are few beside the
-// weight's (16 x 32768 x 8192 69.1 and 55.1 us).
+// A few tokens over a large weight: the time is its way from HBM into the CUs, and the
+// 16 x 16 workgroups, whose waves wait for no barrier, take it fastest (1 x 12288 x 8192
+// fp8 20.1 us, 23.8 us on the best of the other tiles; 1 x 16384 x 8192 25.6 and 32.8; 1 x
+// 60000 x 4096 44.7 and 49.0; 4 x 32768 x 8192 49.0 and 55.4), where their waves' rounds of
+// loads are nearly full (1 x 30000 x 5120, 40 steps in rounds of 32: 35.4 us, 31.0 us by
+// cost) and the tokens' rows are few beside the weight's (16 x 32768 x 8192 68.3 and 55.3
+// us). Below 96 MB the costs above choose; 96 MB is where three weights in turn no longer
+// fit the 256 MB cache, as they were when this was fitted.
 bool streams_weight(int64_t m, int64_t n, int64_t nk)
 {
     constexpr int64_t round = kSkinnyWaves * kSkinnyLoads;
@@ -187,7 +193,7 @@ int plan_linear(const char *fn, int64_t m, int64_t n, int64_t k, int dtype, int 
         if (tm > kMaxTiles / tn)
             continue;
         // beyond two of these workgroups per CU their start and end outweigh the steps (1 x 10240 x 1280, 640 of them:
-        // 6.5 us, 5.5 us on 64 x 64 tiles)
+        // 7.4 us, 6.4 us on 64 x 64 tiles; 6.2 and 5.2 us with the weight in the cache)
         if (t == LT_SKINNY && g_force_linear_tile < 0 && !stream && tm * tn > 2 * cus)
             continue;
         for (int64_t s = 1; s <= (t == LT_SKINNY ? 1 : kMaxSplits); ++s) {

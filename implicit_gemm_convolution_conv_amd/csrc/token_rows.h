@@ -2,9 +2,9 @@
 // of a weight matrix) at a time: the row in registers, sums and maxima over it,
 // and its quantisation to 8 bits.
 //
-// A row of `cols` elements is held by TPR threads (part of a wave, a wave, 4 waves
-// or 16), CH runs of 8 consecutive elements each, run c of thread t at element
-// 8 * (c * TPR + t): every load of a wave covers runs side by side. The row
+// A row of `cols` elements is held by TPR threads (part of a wave, a wave, 4 or 16
+// waves, in the norm's backward pass also 6 or 8), CH runs of 8 consecutive elements
+// each, run c of thread t at element 8 * (c * TPR + t): every load of a wave covers runs side by side. The row
 // is read from memory once; all that follows works on the registers.
 #pragma once
 
